@@ -171,8 +171,10 @@ def _need(t: torch.Tensor, dtype, name: str) -> None:
 # mostly theirs (bare ctypes call and launch: 3 us).
 _ROW_DTYPES = {torch.float32: MSA_F32, torch.bfloat16: MSA_BF16, torch.float16: MSA_F16}
 _U8, _INT32, _INT64, _FLOAT32 = torch.uint8, torch.int32, torch.int64, torch.float32
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream().cuda_stream without the object: 3 us less
+# torch's own bindings where it has them: current_stream().cuda_stream makes an object, 3 us more. A torch without
+# CUDA has neither; the host-only entry points work there.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _at(t: Optional[torch.Tensor], dtype, numel: int, device: int, name: str):
