@@ -483,6 +483,9 @@ size_t msa_dense_attn_workspace_size(const msa_geometry* geo, int32_t B, int32_t
  * B up to 4096. The work is cut into equal spans of key blocks whatever the lengths, and the
  * parts of a row are joined by log-sum-exp, always in the same order.
  *   q          [T][64][128] E4M3, device, 16-B aligned
+ *   softmax_scale  above 0, at most 2^42 (any score but 0 is then beyond what follows). The scores are
+ *              fp32: a weight is off by up to 2^-16 (1 + |z_j|) of itself for that alone, and rows with
+ *              some |z_j| above 2^24 may be NaN
  *   workspace  device, 256-B aligned, >= msa_dense_attn_workspace_size(...) bytes; its contents
  *              matter during the call only, and calls that may overlap need one each
  *   out        [T][64][128] bf16, device, 16-B aligned

@@ -1527,6 +1527,11 @@ __global__ void __launch_bounds__(256) k_dense_join(const DenseParams p) {
 // with tiles of 8, 32 tokens 322 and 386; a 2,048-token prompt at 16K 563 and 680.
 int tile_log2(int32_t max_q_len) { return max_q_len > kTileTok ? 4 : (max_q_len > 1 ? 3 : 0); }
 
+// Scores of |z| up to 2^24 keep their row: an exponent's reference is then rounded to 1, so that the largest P is
+// within a factor of 2 of where it should lie, inside f16. The smallest product of two E4M3 values but 0 is 2^-18, so
+// that a larger scale has no other score in that range, and 3e38 x log2(e) is infinite.
+constexpr float kMostScale = 0x1p42f;
+
 struct Layout {
   size_t rec, ml, o, total;
 };
@@ -1561,7 +1566,7 @@ extern "C" msa_status msa_dense_attn(const msa_geometry* geo, const msa_batch* b
   if (st != MSA_OK) return st;
   if ((st = check_prefill_batch(batch)) != MSA_OK) return st;
   if ((st = check_cache(cache, false, true)) != MSA_OK) return st;
-  if (!(softmax_scale > 0.0f) || !isfinite(softmax_scale)) return MSA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.0f) || !(softmax_scale <= kMostScale)) return MSA_ERR_INVALID_ARG;
   if (batch->B == 0 || batch->T == 0) return MSA_OK;
   if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || cache->num_pages == 0)
     return MSA_ERR_INVALID_ARG;
