@@ -489,7 +489,13 @@ size_t msa_dense_attn_workspace_size(const msa_geometry* geo, int32_t B, int32_t
  *   workspace  device, 256-B aligned, >= msa_dense_attn_workspace_size(...) bytes; its contents
  *              matter during the call only, and calls that may overlap need one each
  *   out        [T][64][128] bf16, device, 16-B aligned
- *   lse        nullable [T][64] fp32, device: ln sum_j exp(z_j), for joining shards of a context
+ *   lse        nullable [T][64] fp32, device: ln sum_j exp(z_j) over the keys that the row sees here.
+ *              Shards of a context join by it, out = sum_s exp(lse_s - lse) out_s, where each shard's call
+ *              has one query token a sequence (a token of a longer query as a sequence of its own, with the
+ *              shard's part of the block table) and seq_lens[b] is the number of the shard's keys that the
+ *              token sees; tokens that see none are left out of the call. With more tokens a sequence a
+ *              shard does not work: positions end at seq_lens[b], so that the last keys of a shard
+ *              before the query would be masked for its earlier tokens
  *   status     nullable; a bad page id sets MSA_ERR_DEVICE_FAULT and zero-fills the rows that
  *              would have read it (lse -inf), an inconsistent batch row sets MSA_ERR_INVALID_ARG
  *              and its rows are left as they are, a device wait that gives up MSA_ERR_TIMEOUT

@@ -448,7 +448,8 @@ def msa_dense_attn(batch: Batch, cache: Cache, q: torch.Tensor, softmax_scale: f
                    workspace: torch.Tensor, lse: Optional[torch.Tensor] = None,
                    status: Optional[torch.Tensor] = None) -> None:
     """Causal attention of q [T, 64, 128] (E4M3 bytes) over the whole cache; out [T, 64, 128] bf16 bits,
-    lse [T, 64] fp32 (natural logarithm) if given."""
+    lse [T, 64] fp32 (natural logarithm) if given. Shards of a context join by lse if each call has one query
+    token a sequence."""
     dev = _current_device()
     n = batch.T * Q_HEADS
     if out.element_size() != 2 or not out.is_contiguous() or out.numel() < n * HEAD_DIM or out.get_device() != dev:
