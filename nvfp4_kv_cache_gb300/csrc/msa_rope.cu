@@ -108,7 +108,7 @@ __device__ __forceinline__ void fill_angles(float (*cs)[2][64], const Rope& r, c
                                             int nt) {
   const int half = r.rot >> 1;
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int t = static_cast<int>(quotient(i, r.half_inv)), j = i - t * half;  // i < 64 tokens x 64
+    const int t = static_cast<int>(quotient(i, r.half_inv)), j = i - t * half;  // i < 17 tokens x 64
     angle(r.inv_freq[j], positions[t0 + t], r.scale, &cs[t][0][j], &cs[t][1][j]);
   }
 }
@@ -494,18 +494,25 @@ bool rows_ok(const void* p, int32_t dtype, int64_t tstride, int64_t hstride) {
 
 bool dtype_ok(int32_t dtype) { return dtype == MSA_F32 || dtype == MSA_BF16 || dtype == MSA_F16; }
 
-// Many rows a half warp (64 bytes a lane: their loads in flight together, one set of angles for all)
-// from one and a half such CTAs an SM on; one row below, so that a few tokens spread over the SMs.
-// 64 bf16 heads, normalised: 160 tokens 3.4 us with many and 2.4 with one, 256 tokens 3.4 and 3.5,
-// 512 tokens 4.8 and 5.3.
+// Many rows a half warp (64 bytes a lane: their loads in flight together, one set of angles for all) from where a row a
+// half warp no longer fits the SMs at once, so that fewer rows spread over them. Where such a CTA's rows are more than 8
+// tokens' (few heads), their angles are its work, and it pays from eight times as many rows or, past 16 tokens, not
+// at all. us with many and with one: 64 normalised heads, half the row turned, 14,592 rows bf16 3.6 and 2.9, fp32
+// 2.8 and 2.7; 16,000 rows bf16 3.6 and 3.6 (without norm 2.8 and 3.1), fp32 3.1 and 3.7; 32,768 rows bf16 5.3 and 6.2,
+// fp32 6.4 and 6.6. 8 bf16 heads (8 tokens) 16,000 rows 4.1 and 3.7, 32,768 rows 6.0 and 6.3. 4 bf16 heads (16) 16,000
+// rows 4.8 and 4.0, 65,536 rows 12.0 and 11.7, 262,144 rows 32.4 and 38.7. One fp32 head (32) 16,384 rows 8.0 and 7.6,
+// 262,144 rows 80.1 and 79.0; one bf16 head (64) 9.5 and 7.6, 81.5 and 79.1.
 template <typename In>
 constexpr int kMany = 8 / sizeof(In);
 template <typename In>
-bool many_rows(int64_t rows) {
-  return 2 * rows >= static_cast<int64_t>(3 * kMany<In> * kRowsAtOnce) * msa_host::kTunedSms;
+bool many_rows(int64_t rows, int32_t heads) {
+  const int tokens = (kMany<In> * kRowsAtOnce + heads - 1) / heads;
+  return tokens <= 16 && rows > static_cast<int64_t>(kCtas * kRowsAtOnce) * msa_host::kTunedSms * (tokens <= 8 ? 1 : 8);
 }
-// A half warp a token from as many CTAs on. bf16 rows, normalised: 2,200 tokens 5.8 us so and 5.3 with a half warp
-// a row, 3,200 tokens 7.3 and 7.0, 4,096 tokens 7.3 and 8.5, 8,192 tokens 11.1 and 14.7.
+// A half warp a token from one and a half such CTAs an SM on. us with a token and with a row a half warp, rows of a
+// packed projection, normalised: bf16 2,200 tokens 6.1 and 5.5, 3,200 7.4 and 7.3, 3,648 7.7 and 8.0, 8,192 12.3 and 16.1;
+// fp32 3,648 tokens 8.8 and 8.8, 4,096 9.0 and 9.5, 8,192 13.9 and 16.5 (no norm, the whole row turned, an FP8 index key:
+// 3,648 9.0 and 8.4, 4,096 9.4 and 9.2, 8,192 14.7 and 15.9).
 bool many_tokens(int64_t n) { return 2 * n >= static_cast<int64_t>(3 * kRowsAtOnce) * msa_host::kTunedSms; }
 
 // Tokens that 16 R consecutive rows of `per` a token can touch, as bytes of angles.
@@ -517,7 +524,7 @@ size_t angle_bytes(const Rope& r, int rows, int per) {
 template <typename In>
 cudaError_t launch_rope(const void* x, int64_t rows, int32_t heads, int64_t ts, int64_t hs, const int32_t* pos,
                         const Rope& r, const float* norm, float eps, uint8_t* out, cudaStream_t stream) {
-  const bool many = many_rows<In>(rows);
+  const bool many = many_rows<In>(rows, heads);
   const int per = many ? kMany<In> * kRowsAtOnce : kRowsAtOnce;
   return msa_host::launch_after_previous(many ? k_rope_fp8<In, kMany<In>> : k_rope_fp8<In, 1>,
                                          dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kThreads),
