@@ -231,8 +231,9 @@ typedef struct msa_kv_rows {
 /* msa_kv_insert with the norm and the rotation on the way: K and the index key are normalised
  * (each with its own weight, NULL for none) and rotated to their token's position, V is taken as
  * it is, and all are quantised as msa_kv_insert quantises, the index key to `index_dtype`. fp32
- * rows with rot_dim 0 and no norm give msa_kv_insert's bytes. An infinity saturates its group's scale
- * and itself, a NaN becomes 0.
+ * rows with rot_dim 0 and no norm give msa_kv_insert's bytes. What is not finite after the norm and
+ * the rotation: in NVFP4 an infinity saturates its group's scale and itself and a NaN becomes 0; in an
+ * FP8 index key an infinity becomes 448 with its sign and a NaN stays one.
  *   positions    [n] int32, device; slots and the rest as msa_kv_insert */
 msa_status msa_rope_kv_insert(const msa_kv_rows* rows, int64_t n, const int32_t* positions,
                               const int64_t* slots, const msa_rope* rope, const float* k_norm,
