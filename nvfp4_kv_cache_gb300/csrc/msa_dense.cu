@@ -999,11 +999,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     *abort_flag = 0;
   }
-  {
-    // the query tiles start as zeros: rows of absent tokens then hold finite values
-    uint4* qz = reinterpret_cast<uint4*>(smem + S::kOffQ);
-    for (int i = tid; i < 2 * S::kQTile / 16; i += kThreads) qz[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
   if (warp == kWarpTmem) tmem_alloc(tmem_slot, S::kTmemCols);
   build_dequant_lut(lut, tid, kThreads);
   fence_proxy_async_smem();
