@@ -482,7 +482,9 @@ size_t msa_dense_attn_workspace_size(const msa_geometry* geo, int32_t B, int32_t
  * E4M3 as in msa_sparse_attn_decode, whose result this is for sequences of at most 16 blocks (up
  * to summation order). Any number of query tokens a sequence: max_q_len up to 2^20, T up to 2^22,
  * B up to 4096. The work is cut into equal spans of key blocks whatever the lengths, and the
- * parts of a row are joined by log-sum-exp, always in the same order.
+ * parts of a row are joined by log-sum-exp, always in the same order. One of three forms is taken
+ * for the whole batch by its max_q_len (1, up to 8, more): a prompt's chunk and many sequences of
+ * one token are faster in a call each.
  *   q          [T][64][128] E4M3, device, 16-B aligned
  *   softmax_scale  above 0, at most 2^42 (any score but 0 is then beyond what follows). The scores are
  *              fp32: a weight is off by up to 2^-16 (1 + |z_j|) of itself for that alone, and rows with

@@ -5,7 +5,8 @@
 // of one sequence (16 where sequences may hold more than 8), its 16 heads a token the rows of the
 // MMAs' M = 128; a unit is one 128-key block of one group's K and V. Units are numbered sequence by
 // sequence, tile by tile, group by group, and cut into equal spans of kTunedSms CTAs, so that every
-// SM streams the same number of blocks whatever the lengths; a (tile, group) cut by a span's border
+// SM streams the same number of blocks whatever the lengths (blocks cost the same where all tiles have one form;
+// a tile of more than 8 tokens costs more a block than one of fewer); a (tile, group) cut by a span's border
 // leaves its parts' unnormalised sums in the workspace and a second kernel joins them, in order.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -410,6 +411,7 @@ __device__ __forceinline__ void dequant_quarter(const RawRow& raw, int q, uint32
 // every role leaves); nothing traps.
 // The roles' order in the source is measured: the hot loops together fill the instruction cache, and
 // other orders of the same code took up to 670 us where this one takes 563 for a 2,048-token prompt.
+// 20 warps leave 96 registers a thread, and k_dense<false> spills 12 bytes, k_dense<true> 16.
 template <bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
     k_dense(const DenseParams p, const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map) {
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  grid_launch_dependents();  // the join's CTAs wait for this grid's end already resident
+  grid_launch_dependents();  // the join's CTAs take the SMs' places as this grid's leave (beside one there is no room)
 
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {  // a warp's bounded wait
     if (warp_wait(bar, parity, abort_flag)) return true;
@@ -878,8 +880,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 //  of scores of standard deviation 2 rescaled, and cost 10 us of a 32 x 32K call.)
 // Two dequant warpgroups take blocks in turn (K rows, then V rows), and two softmax warpgroups, each with
 // its own reference, sum and O^T; these are joined at a segment's end. What bounds it: a 32 x 32K call
-// takes 132 us where its bytes take 89. The integer pipe is 53 % busy (the dequant's permutes: 7
-// instructions for 8 elements), the issue slots 50 %, DRAM 69 %: the dequant warps, two a scheduler, wait for
+// takes 132 us where its bytes take 89. No unit is full: the integer pipe is 53 % busy (the dequant's permutes: 7
+// instructions for 8 elements), the issue slots 56 %, DRAM 69 %; the dequant warps, two a scheduler, wait for
 // their table look-ups. More warps (three warpgroups of either kind, or K and V apart) were slower, by 20 %
 // and more.
 namespace few {
@@ -1008,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  grid_launch_dependents();  // the join's CTAs wait for this grid's end already resident
+  grid_launch_dependents();  // the join's CTAs take the SMs' places as this grid's leave (beside one there is no room)
 
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {  // a warp's bounded wait
     if (warp_wait(bar, parity, abort_flag)) return true;
@@ -1519,7 +1521,9 @@ __global__ void __launch_bounds__(256) k_dense_join(const DenseParams p) {
 // Tokens a tile: 16 (two row tiles, K and V dequantised once for both) where a sequence may hold
 // more than 8, else 8; 1 (k_dense_few) where none holds more. Both sides, 32 sequences of 16K: one token 75 us
 // with k_dense_few and 98 with tiles of 8, two tokens 128 and 100; nine tokens 160 us with tiles of 16 and 198
-// with tiles of 8, 32 tokens 322 and 386; a 2,048-token prompt at 16K 563 and 680.
+// with tiles of 8, 32 tokens 322 and 386; a 2,048-token prompt at 16K 563 and 680. The rule is the batch's, not a
+// sequence's: 31 sequences of one token at 32K take 127 us by themselves, 173 with tiles of 8 and 189 with tiles of 16,
+// and in one batch with a 2,048-token chunk at 16K 826 us, where the two calls take 692.
 int tile_log2(int32_t max_q_len) { return max_q_len > kTileTok ? 4 : (max_q_len > 1 ? 3 : 0); }
 
 // Scores of |z| up to 2^24 keep their row: an exponent's reference is then rounded to 1, so that the largest P is

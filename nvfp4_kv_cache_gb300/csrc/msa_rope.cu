@@ -7,8 +7,10 @@
 // NVFP4 scale are shuffles inside the half warp; a query row's elements lie as the rotation pairs them up,
 // a cache row's in order (its codes and scales are groups of neighbours) and its partners come by shuffles. The
 // cosines and sines of a token are computed once per CTA (they are the same for all its heads).
-// What bounds them: the queries their bytes (8,192 x 64 f16 rows: 35.7 us, 5.65 TB/s), the append and the
-// read-back their instructions (16,383 tokens from fp32 rows: 24 and 11 us, where their bytes take 13 and 4.4).
+// What bounds them: the queries their bytes where a lane's pieces are neighbours (8,192 x 64 f16 rows, interleaved pairs:
+// 35.4 us, 5.69 TB/s); in the half layout they are apart, and loads and stores touch sectors twice (bf16, normalised: 48 us,
+// 4.2 TB/s). The append and the read-back their instructions (16,383 tokens from fp32 rows: 23 and 14 us, where their bytes
+// take 13 and 4.4; 8,192 from bf16 rows: 12 us, 3.6).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -27,8 +29,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowsAtOnce = kThreads / 16;
 // Resident CTAs an SM: the kernels wait for memory, then for their angles (8,192 x 64 f16 rows: 35.7 us
-// with six, 37.2 with five). The insert by tokens holds four rows (16,383
-// tokens and their read-back: 34.6 us with four, 36.7 with three, 43.2 with five, which spills).
+// with six, 37.2 with five; six leave 40 registers, and four rows of 16 bits spill 32 bytes). The insert by tokens
+// holds four rows (16,383 tokens and their read-back: 34.6 us with four, where fp32 rows spill 16 bytes, 36.7 with
+// three, 43.2 with five, which spills more).
 constexpr int kCtas = 6, kInsertCtas = 5, kTokenCtas = 4;
 
 // i / d by a product and a shift: d_inv = 2^22 / d rounded up, exact where i d < 2^22 (a division is some
